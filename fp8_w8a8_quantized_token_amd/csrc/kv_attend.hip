@@ -21,7 +21,10 @@
 //     p' = 2^(score * log2 e + log2(v_scale) - m), so that O^T sums p' times V codes and
 //     needs no scaling by pages; the denominator sums p' / v_scale. m is a bound, not the
 //     maximum: it moves (and O and l are rescaled) only when a lane's p' of a tile sum to
-//     more than 2^40, so that a tile needs no maximum.
+//     more than 2^40, or its p' / v_scale to more than 2^90, so that a tile needs no maximum.
+//     It moves to the largest score * log2 e + max(log2(v_scale), -60): p' is then at most 1 and
+//     p' / v_scale at most 2^60, whatever V scales a request holds, and the denominator of 2^30
+//     tokens stays within fp32 with its inverse.
 //   * Output: p' is rounded once to bf16, which keeps 8 bits over the whole range of fp32
 //     (fp16 would keep 11, but lose what lies 2^-32 below a row's largest, all there is in a
 //     column whose strongest tokens hold zero); the denominator is a sum in fp32 (see powers).
@@ -43,7 +46,9 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 constexpr int kTile = 64;          // tokens of a score tile
 constexpr float kNone = -1e30f;    // the running maximum before any token
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMost = 0x1p40f;   // a lane's p' of a tile may sum to this before m moves
+constexpr float kMost = 0x1p40f;   // a lane's p' of a tile may sum to this before m moves,
+constexpr float kWeight = 0x1p-50f;  // and its p' / v_scale, its share of the denominator, to kMost / kWeight
+constexpr float kLeastLog = -60.0f;  // of a V scale's logarithm in the bound
 
 struct AttendArgs {
   KvCache c;
@@ -128,11 +133,11 @@ __device__ __forceinline__ void softmax_step(bool first, const Scores& s, float 
                                              float& m, float& l, const Over& over, const Rescale& rescale) {
   float sum = INFINITY;
   if (!first) sum = powers<N, DOTS>(s, c, lv - m, p);
-  if (__builtin_expect(__any(!(sum <= kMost)), 0)) {
+  if (__builtin_expect(__any(!(fmaxf(sum, sum * rv * kWeight) <= kMost)), 0)) {
     float mx = s(0);
 #pragma unroll
     for (int e = 1; e < N; ++e) mx = fmaxf(mx, s(e));
-    const float up = fmaxf(m, over(__builtin_fmaf(mx, c, lv)));
+    const float up = fmaxf(m, over(__builtin_fmaf(mx, c, fmaxf(lv, kLeastLog))));
     const float fix = __builtin_amdgcn_exp2f(m - up);
     m = up;
     l *= fix;

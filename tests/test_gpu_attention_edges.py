@@ -1,0 +1,49 @@
+"""The attention step at the edges of what its entry points take: value scales at the ends of
+their range, values that do not depend on the weights, and rows that stand at odd addresses."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import e4m3
+from tests._helpers import bf16_out_to_f64, require_gpu
+from tests.test_gpu_kv_cache import attend, make, reference
+
+pytestmark = pytest.mark.gpu
+
+# (rows, head dimension): tiles of 16 rows, of 128, and of 256
+FORMS = [(1, 64), (1, 128), (300, 64), (300, 128)]
+
+
+def code_of(x):
+    return int(e4m3.encode(np.array([x], np.float32))[0])
+
+
+def assert_weighted(got, ref, weight):
+    """One rounding of each weight, shared by the sum that divides them, moves an output by up to
+    2^-8 sum_j p_j |v_j - out| <= 2^-7 weight, its own rounding by 2^-8 of it; exponents of up to
+    2^7 in fp32 are off by less than 2^-15."""
+    err = np.abs(bf16_out_to_f64(got) - ref)
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -15) * weight
+    assert np.all(err <= bound), float(np.nanmax(err / (bound + 1e-300)))
+
+
+@pytest.mark.parametrize("page", [32, 64, 128])
+@pytest.mark.parametrize("count,dim", FORMS)
+@pytest.mark.parametrize("lead,early,late", [(39, -100, -100), (30, -100, -100), (38, -90, -90), (39, -60, -60),
+                                             (130, 0, -100), (39, -100, 0), (100, 20, -80), (20, 100, 100)])
+def test_value_scales_at_the_ends_of_their_range(lead, early, late, count, dim, page):
+    """Scores of later pages `lead` powers of two above those of the first 512 places, V scales 2^early and 2^late."""
+    dev = require_gpu()
+    c = make([count], [1300], 2, 1, dim, page, seed=40)
+    c["q"].zero_()
+    c["q"][..., 0] = 1.0
+    c["k"][:] = 0
+    for j, p in enumerate(c["table"][0, :-(-1300 // page)]):
+        first = j * page < 512
+        c["vs"][p], c["ks"][p] = 2.0 ** (early if first else late), 1.0 if first else lead
+        if not first:
+            c["k"][p, :, 5, 0] = code_of(1.0)
+    scale = float(np.float32(np.log(2.0)))  # a score of 1 is a power of two
+    for causal in (False, True):
+        assert_weighted(attend(c, dev, causal, scale=scale), *reference(c, causal, scale))
