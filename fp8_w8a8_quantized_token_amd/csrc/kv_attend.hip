@@ -88,14 +88,15 @@ __device__ __forceinline__ v8bf widen(int w0, int w1) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// p' of a lane's N scores, rounded to bf16, and their sum: of the rounded ones (the weights of a
-// row then sum to one) by two-element dot products, or, DOTS false, of p' as it was by additions.
-// The dot products go through the matrix cores: beside another wavefront's products one takes
-// 38 cycles, two additions 10. Where a wavefront's softmax runs beside such products all the time
-// (kv_attend_teams) the additions are 3% faster (32760 x 32760, 16 heads of 128: 7.22 -> 6.97 ms;
-// 1560 x 32760: 440 -> 428 us), at an error of 2.3e-3 of the output's norm against 1.9e-3, 1.7e-3
-// of it the output's own rounding; elsewhere they gain nothing (6 ragged causal requests, 32
-// heads of 64: 123 us against 120).
+// p' of a lane's N scores, rounded to bf16, and the sum of the rounded ones: the weights of a row
+// then sum to one, and values that are all alike come back as they are (with the sum of the
+// unrounded ones a row that one token rules is off by up to 2^-8 in all its columns). By
+// two-element dot products, or, DOTS false, by additions of the widened halves: the dot products go
+// through the matrix cores, and beside another wavefront's products one takes 38 cycles, two
+// additions and the widening 20. Where a wavefront's softmax runs beside such products all the time
+// (kv_attend_teams) the additions are quicker (32760 x 32760, 16 heads of 128: 7.33 ms against 7.47;
+// 1560 x 32760: 438 us against 453), elsewhere the dot products (6 ragged causal requests, 32 heads
+// of 64: 123 us against 132). Sums of the unrounded p' would take 7.08 ms and 423 us.
 template <int N, bool DOTS, class Scores>
 __device__ __forceinline__ float powers(const Scores& s, float c, float add, v8bf (&p)[N / 8]) {
   float sum[2] = {0.0f, 0.0f};
@@ -108,8 +109,9 @@ __device__ __forceinline__ float powers(const Scores& s, float c, float add, v8b
       const v2bf16 one = {(__bf16)1.0f, (__bf16)1.0f};
       sum[e / 2 % 2] = __builtin_amdgcn_fdot2_f32_bf16(h, one, sum[e / 2 % 2], false);
     } else {
-      sum[0] += x;
-      sum[1] += y;
+      const uint32_t w = __builtin_bit_cast(uint32_t, h);
+      sum[0] += __uint_as_float(w << 16);
+      sum[1] += __uint_as_float(w & 0xffff0000u);
     }
     p[e / 8][e % 8] = h[0];
     p[e / 8][e % 8 + 1] = h[1];

@@ -572,7 +572,9 @@ int fp8_kv_append(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, c
  *
  * over the places j < lengths[i] of the row's request, or, where causal, j <= lengths[i] -
  * n + (row within the request); k and v are those of cache head h / (heads / cache heads).
- * Scores, softmax and sums are fp32. A row with no place to look at gives zeros. Whatever
+ * Scores, exponentials and sums are fp32; p_j v_scale is rounded once to bf16 before the
+ * products with the codes of V, and the sum that divides them is that of the rounded ones, so
+ * that the weights of a row sum to one. A row with no place to look at gives zeros. Whatever
  * stands in slots that a row does not see, NaN codes and the scales of pages it sees nothing
  * of included, has no effect on it. Queries and what a row sees must be finite, and the V
  * scales of one request at least 2^-100 and within 2^100 of each other.

@@ -47,3 +47,20 @@ def test_value_scales_at_the_ends_of_their_range(lead, early, late, count, dim, 
     scale = float(np.float32(np.log(2.0)))  # a score of 1 is a power of two
     for causal in (False, True):
         assert_weighted(attend(c, dev, causal, scale=scale), *reference(c, causal, scale))
+
+
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("count,length,heads,kv_heads,dim", [(1, 1300, 4, 2, 64), (1, 5000, 4, 2, 128), (40, 1300, 4, 2, 128),
+                                                             (300, 1300, 4, 2, 64), (300, 1300, 4, 2, 128),
+                                                             (1100, 2000, 64, 64, 128), (2000, 2000, 4, 4, 128)])
+def test_equal_values_come_back_whatever_the_weights(count, length, heads, kv_heads, dim, page):
+    """The weights of a row sum to one: of values that are all 1.5 (as 1.5 * 1 and as 3 * 0.5) the result is 1.5,
+    with nothing but fp32 sums (2^-13 at these lengths) in between, and 2^-8 away from the next result."""
+    dev = require_gpu()
+    c = make([count], [length], heads, kv_heads, dim, page, seed=41)
+    c["q"] *= 3
+    for j, p in enumerate(c["table"][0, :-(-length // page)]):
+        c["v"][p], c["vs"][p] = code_of(3.0 if j % 2 else 1.5), 0.5 if j % 2 else 1.0
+    for causal in (False, True):
+        got = attend(c, dev, causal)
+        assert bool((got == 1.5).all()), float((got.float() - 1.5).abs().max())
