@@ -256,8 +256,8 @@ class Fp8KVCache:
             _on_device(self.device, workspace=workspace)
         if requests == 0 or tokens == 0:
             return out
-        if table_pages == 0:  # no places at all
-            return out.zero_()
+        if table_pages == 0:  # no places at all: one page that is not named, so that rows of no request are left
+            table, table_pages = torch.full((requests, 1), -1, dtype=_int32, device=self.device), 1
         q, q_words = _packed(q)
         if workspace is None:
             need = self.workspace_bytes(requests, tokens, heads, table_pages)

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import fp8_w8a8_quantized_token_amd as fp8
 from oracle import e4m3
 from tests._helpers import bf16_out_to_f64, require_gpu
 from tests.test_gpu_kv_cache import attend, make, reference
@@ -64,3 +65,14 @@ def test_equal_values_come_back_whatever_the_weights(count, length, heads, kv_he
     for causal in (False, True):
         got = attend(c, dev, causal)
         assert bool((got == 1.5).all()), float((got.float() - 1.5).abs().max())
+
+
+def test_no_table_leaves_rows_of_no_request():
+    dev = require_gpu()
+    cache = fp8.Fp8KVCache(2, 2, device=dev)
+    table = torch.empty((2, 0), dtype=torch.int32, device=dev)
+    lengths, starts = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([4, 4], [2, 3, 6]))
+    q = torch.ones((9, 4, 128), dtype=torch.bfloat16, device=dev)
+    out = torch.full_like(q, 7.0)
+    assert cache.attend(q, table, lengths, starts, out=out) is out
+    assert not out[2:6].any() and bool((out[:2] == 7).all()) and bool((out[6:] == 7).all())
