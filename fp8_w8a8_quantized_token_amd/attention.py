@@ -67,10 +67,15 @@ def _rows(t, name, device=None, heads=None, dim=None):
 
 def _words(t):
     """A tensor's fp8_rows, or None if the library cannot take it in place (dense 16-byte aligned rows)."""
+    tokens, heads, dim = t.shape
     token, head, column = t.stride()
+    if tokens == 1:  # a stride that is never stepped may be anything
+        token = dim
+    if heads == 1:
+        head = dim
     at = t.data_ptr()
     if column == 1 and token % 8 == 0 and head % 8 == 0 and at % 16 == 0:
-        return _pack_rows(at, t.shape[1], token, head)
+        return _pack_rows(at, heads, token, head)
     return None
 
 
@@ -78,8 +83,9 @@ def _packed(t):
     """(tensor, its fp8_rows): a dense copy where it cannot be taken in place. The caller holds it until the launch."""
     words = _words(t)
     if words is None:
-        t = t.contiguous()
-        words = _pack_rows(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+        # not .contiguous(): a dense tensor at an odd address would come back as it is
+        t = t.clone(memory_format=torch.contiguous_format)
+        words = _pack_rows(t.data_ptr(), t.shape[1], t.shape[1] * t.shape[2], t.shape[2])
     return t, words
 
 

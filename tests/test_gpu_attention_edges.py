@@ -76,3 +76,50 @@ def test_no_table_leaves_rows_of_no_request():
     out = torch.full_like(q, 7.0)
     assert cache.attend(q, table, lengths, starts, out=out) is out
     assert not out[2:6].any() and bool((out[:2] == 7).all()) and bool((out[6:] == 7).all())
+
+
+def at_odd_columns(x, dev, column):
+    """x [tokens, heads, dim] as columns of a wider tensor, from this one on."""
+    tokens, heads, dim = x.shape
+    wide = torch.zeros((tokens, column + heads * dim + 3), dtype=x.dtype, device=dev)
+    wide[:, column:column + heads * dim] = x.reshape(tokens, -1)
+    return wide[:, column:column + heads * dim].unflatten(1, (heads, dim))
+
+
+@pytest.mark.parametrize("tokens", [1, 2])
+@pytest.mark.parametrize("heads", [1, 2])
+@pytest.mark.parametrize("column", [0, 4, 8, 9])
+def test_rows_at_any_address(column, heads, tokens):
+    """A layer that works for a prompt works for its single-token steps: slices that begin anywhere."""
+    dev = require_gpu()
+    rng = torch.Generator().manual_seed(42)
+    q, k, v = (torch.randn((tokens, heads, 128), generator=rng).to(torch.bfloat16) for _ in range(3))
+    pos = torch.arange(3 * tokens, dtype=torch.int32, device=dev).view(tokens, 3)
+    rope = fp8.RopeAxes(128, (16, 56, 56))
+    whole = [x.to(dev) for x in (q, k, v)]
+    odd = [at_odd_columns(x, dev, column) for x in (q, k, v)]
+    for got, want in zip(rope(odd[0], odd[1], pos), rope(whole[0], whole[1], pos)):
+        assert torch.equal(got, want)
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device=dev)
+    lengths, starts = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([tokens], [0, tokens]))
+    outs = []
+    for x in (whole, odd):
+        cache = fp8.Fp8KVCache(2, heads, device=dev)
+        cache.append(x[1], x[2], table, lengths, starts)
+        outs.append((cache.attend(x[0], table, lengths, starts), cache.k_codes[1, :, :tokens], cache.v_codes[1, :, :, :tokens],
+                     cache.k_scale[1], cache.v_scale[1]))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_strides_of_single_rows_do_not_matter():
+    """A dimension of size one may have any stride, of an input and of an output."""
+    dev = require_gpu()
+    rope = fp8.RopeAxes(64, (32, 32))
+    pos = torch.tensor([[3, 5]], dtype=torch.int32, device=dev)
+    x = torch.randn((1, 1, 64), device=dev).to(torch.bfloat16)
+    want = rope(x, None, pos)[0]
+    for token, head in ((1, 64), (64, 3), (0, 0), (7, 7)):
+        out = torch.zeros(64, dtype=torch.bfloat16, device=dev).as_strided((1, 1, 64), (token, head, 1))
+        got = rope(x.view(64).as_strided((1, 1, 64), (token, head, 1)), None, pos, q_out=out)[0]
+        assert got is out and torch.equal(got, want)
