@@ -78,7 +78,7 @@ __global__ __launch_bounds__(PAGE* DIM / 32) void kv_append_kernel(AppendArgs a)
   constexpr int kWaves = kThreads / 64;
   constexpr int kChunks = DIM / 8;
   __shared__ float wave_amax[2][kWaves];
-  __shared__ uint32_t turned[DIM * PAGE / 4];
+  __shared__ __attribute__((aligned(16))) uint32_t turned[DIM * PAGE / 4];
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kShift = __builtin_ctz(PAGE);
   const int head = blockIdx.y;
