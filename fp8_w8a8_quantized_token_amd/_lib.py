@@ -6,6 +6,7 @@ import of any op raises; nothing here computes anything itself.
 
 import ctypes
 import os
+import struct
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libfp8w8a8.so")
@@ -53,6 +54,10 @@ class Rows(ctypes.Structure):
     """fp8_rows: a bf16 [tokens, heads, head_dim] tensor with strides in elements."""
 
     _fields_ = [("data", _c_p), ("heads", _c_i64), ("token_stride", _c_i64), ("head_stride", _c_i64)]
+
+
+# The same structure as packed bytes, which a call takes as quickly as an address.
+pack_rows = struct.Struct("".join({_c_p: "P", _c_i64: "q"}[kind] for _, kind in Rows._fields_)).pack
 
 
 # name -> (restype, argtypes); every function declared in include/fp8w8a8.h

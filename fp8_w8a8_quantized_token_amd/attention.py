@@ -9,11 +9,10 @@ read by the kernels only, so no call waits for the GPU and all of them can be ca
 """
 
 import ctypes
-import struct
 
 import torch
 
-from ._lib import ROPE_HALVES, ROPE_INTERLEAVED, check, lib
+from ._lib import ROPE_HALVES, ROPE_INTERLEAVED, check, lib, pack_rows
 from .ops import _on_device, _ptr, _require
 
 # The calls that serve single tokens take a few microseconds on the GPU, so the way there is
@@ -21,7 +20,6 @@ from .ops import _on_device, _ptr, _require
 # the device is only changed where it is another one.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_pack_rows = struct.Struct("4q").pack  # an fp8_rows: data, heads, token_stride, head_stride
 _int32, _bf16 = torch.int32, torch.bfloat16
 
 
@@ -75,7 +73,7 @@ def _words(t):
         head = dim
     at = t.data_ptr()
     if column == 1 and token % 8 == 0 and head % 8 == 0 and at % 16 == 0:
-        return _pack_rows(at, heads, token, head)
+        return pack_rows(at, heads, token, head)
     return None
 
 
@@ -85,7 +83,7 @@ def _packed(t):
     if words is None:
         # not .contiguous(): a dense tensor at an odd address would come back as it is
         t = t.clone(memory_format=torch.contiguous_format)
-        words = _pack_rows(t.data_ptr(), t.shape[1], t.shape[1] * t.shape[2], t.shape[2])
+        words = pack_rows(t.data_ptr(), t.shape[1], t.shape[1] * t.shape[2], t.shape[2])
     return t, words
 
 
