@@ -186,6 +186,8 @@ class Fp8KVCache:
             if pages is None or heads is None:
                 raise ValueError("Fp8KVCache needs pages and heads, or a pool's tensors")
             device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+            if device.type != "cuda":
+                raise ValueError(f"the pool must be on a GPU (the HIP library is the only implementation), not {device}")
             k_codes = torch.empty((pages, heads, page_tokens, head_dim), dtype=torch.uint8, device=device)
             v_codes = torch.empty((pages, heads, head_dim, page_tokens), dtype=torch.uint8, device=device)
             k_scale = torch.empty((pages, heads), dtype=torch.float32, device=device)
