@@ -57,13 +57,17 @@ int check_batch(int64_t requests, int64_t tokens) {
   return FP8W8A8_OK;
 }
 
+bool table_fits(const KvCache& c, int64_t table_pages) {
+  return table_pages >= 1 && table_pages <= FP8W8A8_MAX_PLACES / c.page_tokens;
+}
+
 // The ragged batch of a cache call: request lengths, row offsets and the page table.
 int check_paged(const KvCache& c, int64_t requests, int64_t tokens, const int32_t* table, int64_t table_pages,
                 const int32_t* lengths, const int32_t* starts) {
   if (!table || !lengths || !starts) return FP8W8A8_ERR_INVALID_ARG;
   const int st = check_batch(requests, tokens);
   if (st != FP8W8A8_OK) return st;
-  if (table_pages < 1 || table_pages * c.page_tokens > FP8W8A8_MAX_PLACES) return FP8W8A8_ERR_BAD_SHAPE;
+  if (!table_fits(c, table_pages)) return FP8W8A8_ERR_BAD_SHAPE;
   if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(starts, 4)) return FP8W8A8_ERR_MISALIGNED;
   return FP8W8A8_OK;
 }
@@ -183,7 +187,8 @@ int fp8_kv_append(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, c
 
 size_t fp8_kv_attend_workspace_bytes(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, int64_t heads,
                                      int64_t table_pages) {
-  if (!cache || requests <= 0 || tokens <= 0 || heads <= 0 || table_pages <= 0) return 0;
+  if (!cache || requests <= 0 || tokens <= 0 || check_batch(requests, tokens) != FP8W8A8_OK) return 0;
+  if (heads < 1 || heads > kMaxHeads || heads % cache->c.heads != 0 || !table_fits(cache->c, table_pages)) return 0;
   return kv_attend_workspace_bytes(
       cache->c, kv_attend_cut(cache->c, requests, tokens, heads, table_pages, cache->cu_count), heads);
 }

@@ -586,7 +586,8 @@ int fp8_kv_append(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, c
  *              overlap with q
  *   workspace  device, 256-byte aligned, at least fp8_kv_attend_workspace_bytes(cache,
  *              requests, tokens, heads, table_pages) bytes, no initialisation needed; may be
- *              NULL where that is 0. Two calls that overlap in time must not share it.
+ *              NULL where that is 0 (as it is for sizes that the call refuses). Two calls that
+ *              overlap in time must not share it.
  */
 size_t fp8_kv_attend_workspace_bytes(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, int64_t heads,
                                      int64_t table_pages);

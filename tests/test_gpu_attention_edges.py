@@ -1,11 +1,14 @@
 """The attention step at the edges of what its entry points take: value scales at the ends of
 their range, values that do not depend on the weights, and rows that stand at odd addresses."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import fp8_w8a8_quantized_token_amd as fp8
+from fp8_w8a8_quantized_token_amd import _lib
 from oracle import e4m3
 from tests._helpers import bf16_out_to_f64, require_gpu
 from tests.test_gpu_kv_cache import attend, make, reference
@@ -123,3 +126,21 @@ def test_strides_of_single_rows_do_not_matter():
         out = torch.zeros(64, dtype=torch.bfloat16, device=dev).as_strided((1, 1, 64), (token, head, 1))
         got = rope(x.view(64).as_strided((1, 1, 64), (token, head, 1)), None, pos, q_out=out)[0]
         assert got is out and torch.equal(got, want)
+
+
+def test_tables_whose_places_pass_64_bits_are_refused():
+    dev = require_gpu()
+    cache = fp8.Fp8KVCache(2, 2, device=dev)
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16, device=dev)
+    table = torch.zeros((1, 1), dtype=torch.int32, device=dev)
+    lengths, starts = (torch.tensor(n, dtype=torch.int32, device=dev) for n in ([1], [0, 1]))
+    rows = ctypes.byref(_lib.Rows(x.data_ptr(), 2, 256, 128))
+    for pages in ((1 << 58) + 1, (1 << 62) + 1, (1 << 24) + 1):  # times 64 places
+        assert _lib.lib().fp8_kv_append(cache._cache, 1, 1, rows, rows, table.data_ptr(), pages, lengths.data_ptr(),
+                                        starts.data_ptr(), None) == _lib.ERR_BAD_SHAPE
+        assert _lib.lib().fp8_kv_attend(cache._cache, 1, 1, rows, table.data_ptr(), pages, lengths.data_ptr(),
+                                        starts.data_ptr(), 1.0, 0, x.data_ptr(), None, 0, None) == _lib.ERR_BAD_SHAPE
+        assert cache.workspace_bytes(1, 1, 2, pages) == 0
+    for refused in ((1 << 62, 1, 2, 9), (1, 1 << 62, 2, 9), (1, 1, 3, 9), (1, 1, 1 << 62, 9)):
+        assert cache.workspace_bytes(*refused) == 0
+    assert cache.workspace_bytes(1, 1, 2, 1 << 10) > 0
