@@ -1033,6 +1033,7 @@ AttendCut kv_attend_cut(const KvCache& c, int64_t requests, int64_t tokens, int6
     const int64_t spread = std::min<int64_t>(tiles / 8, cus / busy);
     const int64_t even = requests > 1 ? std::min<int64_t>(tiles / 16, 16 * (int64_t)cus / busy) : 1;
     x.parts = (int)std::min<int64_t>(std::max<int64_t>({1, spread, even}), kMaxParts);
+    while (x.parts > 1 && !kv_attend_fits(c, x, tokens, heads)) --x.parts;
     return x;
   }
   // In tiles' time. Heads of 128: rounds of one workgroup to a CU, each its share of the tiles
@@ -1051,22 +1052,25 @@ AttendCut kv_attend_cut(const KvCache& c, int64_t requests, int64_t tokens, int6
   const int64_t full = requests == 1 ? busy / at_once * at_once / c.heads : 0;
   double best = 0;
   x.parts = 1;
+  AttendCut y = x;
   for (int64_t whole : {(int64_t)0, full}) {
     const int64_t units = busy - whole * c.heads;
     const double before = whole ? rounds(whole * c.heads, 1) + 4 : 0;
     if (units <= 0 || (whole && whole >= x.slots)) continue;
+    y.whole = whole;
+    if (whole) y.part_rows = std::min(tokens, (((x.slots - whole) << x.shift) + group - 1) / group);
     for (int p = whole ? 2 : 1; p <= 32 && p <= std::max<int64_t>(1, tiles / 4); ++p) {
       const double rows = (double)units / busy * (double)tokens;
       const double join = p == 1 ? 0 : 2 + 1.3e-4 * p * rows * (double)heads;
       const double time = before + rounds(units, p) + join;
-      if ((p == 1 && !whole) || time < best) {
+      y.parts = p;
+      // parts never make a call too large that fits without
+      if ((p == 1 && !whole) || (time < best && kv_attend_fits(c, y, tokens, heads))) {
         best = time;
-        x.parts = p;
-        x.whole = whole;
+        x = y;
       }
     }
   }
-  if (x.whole) x.part_rows = std::min(tokens, (((x.slots - x.whole) << x.shift) + group - 1) / group);
   return x;
 }
 

@@ -144,3 +144,23 @@ def test_tables_whose_places_pass_64_bits_are_refused():
     for refused in ((1 << 62, 1, 2, 9), (1, 1 << 62, 2, 9), (1, 1, 3, 9), (1, 1, 1 << 62, 9)):
         assert cache.workspace_bytes(*refused) == 0
     assert cache.workspace_bytes(1, 1, 2, 1 << 10) > 0
+
+
+def test_parts_do_not_make_a_call_too_large():
+    """Sizes of which a cut into parts would be more than a launch holds are served without."""
+    dev = require_gpu()
+    requests, tokens = 1170, (1 << 24) - 1
+    cache = fp8.Fp8KVCache(1, 2, device=dev)
+    row = torch.randn((1, 2, 128), device=dev).to(torch.bfloat16)
+    starts, lengths = (torch.zeros(n, dtype=torch.int32, device=dev) for n in (requests + 1, requests))
+    starts[-1] = lengths[-1] = 5  # the last request has five rows, the others none
+    table = torch.full((requests, 308278), -1, dtype=torch.int32, device=dev)
+    table[-1, 0] = 0
+    five = row.expand(5, 2, 128)
+    cache.append(five, five, table[-1:], lengths[-1:], starts[-2:])
+    out = torch.empty((tokens, 2, 128), dtype=torch.bfloat16, device=dev)
+    out[5:9] = 7.0
+    assert cache.workspace_bytes(requests, tokens, 2, table.shape[1]) == 0
+    cache.attend(row.expand(tokens, 2, 128), table, lengths, starts, out=out)
+    assert torch.equal(out[:5], cache.attend(five, table[-1:], lengths[-1:], starts[-2:]))
+    assert bool((out[5:9] == 7).all())
