@@ -42,6 +42,7 @@ MAX_GROUP = 4
 MAX_DIM = 1 << 20
 MAX_AXES = 4
 MAX_RANK = 128
+MAX_REQUESTS = 1 << 20
 
 ROPE_INTERLEAVED = 0
 ROPE_HALVES = 1

@@ -30,7 +30,7 @@ namespace {
 
 constexpr int64_t kMaxGridThreads = (int64_t)1 << 32;
 constexpr int64_t kMaxHeads = 65535;      // a grid dimension
-constexpr int64_t kMaxRequests = 1 << 20;
+constexpr int64_t kMaxRequests = FP8W8A8_MAX_REQUESTS;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -189,8 +189,8 @@ size_t fp8_kv_attend_workspace_bytes(const fp8_kv_cache* cache, int64_t requests
                                      int64_t table_pages) {
   if (!cache || requests <= 0 || tokens <= 0 || check_batch(requests, tokens) != FP8W8A8_OK) return 0;
   if (heads < 1 || heads > kMaxHeads || heads % cache->c.heads != 0 || !table_fits(cache->c, table_pages)) return 0;
-  return kv_attend_workspace_bytes(
-      cache->c, kv_attend_cut(cache->c, requests, tokens, heads, table_pages, cache->cu_count), heads);
+  const AttendCut cut = kv_attend_cut(cache->c, requests, tokens, heads, table_pages, cache->cu_count);
+  return kv_attend_fits(cache->c, cut, tokens, heads) ? kv_attend_workspace_bytes(cache->c, cut, heads) : 0;
 }
 
 int fp8_kv_attend(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, const fp8_rows* q, const int32_t* table,

@@ -461,7 +461,8 @@ int fp8_w8a16_run_config(int config_id, int w_format, int64_t m, int64_t n, int6
  *
  * Ragged batches. The tokens of several requests stand one request after another:
  * request i owns the rows starts[i] .. starts[i + 1] - 1, with starts int32
- * [requests + 1] on the device, ascending. Rows outside every request are not written.
+ * [requests + 1] on the device, ascending, and requests at most FP8W8A8_MAX_REQUESTS. Rows
+ * outside every request are not written.
  * Lengths, offsets, page numbers and adapter numbers are read on the GPU only, so a call
  * never waits for them and may be captured into a graph and replayed with new ones. They
  * cannot be checked on the host: offsets outside 0..tokens are held to that range, and
@@ -471,6 +472,7 @@ int fp8_w8a16_run_config(int config_id, int w_format, int64_t m, int64_t n, int6
  * others with strides in elements (a slice of a fused projection's output is one). data
  * is 16-byte aligned and both strides are multiples of 8.
  */
+#define FP8W8A8_MAX_REQUESTS (1 << 20)
 typedef struct fp8_rows {
   void* data;
   int64_t heads;        /* 1 .. 65535 */
@@ -510,6 +512,7 @@ int fp8_rope_create(int64_t head_dim, int axes, const int64_t* widths, double ba
  *   q, q_out   the queries and where they go, equal heads; q_out may be q itself (in place)
  *              or must not overlap it. An output's strides are at least head_dim.
  *   k, k_out   the same for the keys, any number of heads; both NULL for none
+ * A launch holds fewer than 2^26 rows: tokens times the heads of q and k together.
  */
 int fp8_rope_run(const fp8_rope_plan* plan, int64_t tokens, const int32_t* positions, const fp8_rows* q,
                  const fp8_rows* q_out, const fp8_rows* k, const fp8_rows* k_out, void* stream);
@@ -576,10 +579,14 @@ int fp8_kv_append(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, c
  * products with the codes of V, and the sum that divides them is that of the rounded ones, so
  * that the weights of a row sum to one. A row with no place to look at gives zeros. Whatever
  * stands in slots that a row does not see, NaN codes and the scales of pages it sees nothing
- * of included, has no effect on it. Queries and what a row sees must be finite, and the V
- * scales of one request at least 2^-100 and within 2^100 of each other.
+ * of included, has no effect on it. Queries and what a row sees must be finite (a NaN among it
+ * may reach the output or not), the scales of both above 0, and the V scales of one request
+ * between 2^-100 and 2^119 and within 2^100 of each other.
  *
- *   q          fp8_rows, heads a multiple of the cache's
+ *   q          fp8_rows, heads a multiple of the cache's. A launch holds fewer than 2^23
+ *              workgroups: tokens * heads / 16 + requests * cache heads up to 2^22 always fits,
+ *              with more than 64 rows a request about ten times that; what does not is
+ *              FP8W8A8_ERR_BAD_SHAPE.
  *   scale      finite, above 0
  *   causal     0 or not
  *   out_bf16   device, bf16 [tokens, heads, head_dim] dense, 16-byte aligned, written; no

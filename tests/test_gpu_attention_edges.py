@@ -164,3 +164,22 @@ def test_parts_do_not_make_a_call_too_large():
     cache.attend(row.expand(tokens, 2, 128), table, lengths, starts, out=out)
     assert torch.equal(out[:5], cache.attend(five, table[-1:], lengths[-1:], starts[-2:]))
     assert bool((out[5:9] == 7).all())
+
+
+def test_calls_beyond_the_limits_are_refused():
+    """On the host, whatever the addresses: more requests, or more workgroups, than the header allows."""
+    dev = require_gpu()
+    cache = fp8.Fp8KVCache(2, 2, device=dev)
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16, device=dev)
+    ints = torch.zeros(2, dtype=torch.int32, device=dev)
+    lib, at = _lib.lib(), ints.data_ptr()
+
+    def run(requests, tokens, heads):
+        rows = ctypes.byref(_lib.Rows(x.data_ptr(), heads, 0, 0))
+        return lib.fp8_kv_attend(cache._cache, requests, tokens, rows, at, 1, at, at, 1.0, 0, x.data_ptr(), None, 0, None)
+
+    for requests, tokens, heads in ((_lib.MAX_REQUESTS + 1, 1, 2), (1, _lib.MAX_ROWS - 1, 65534), (1, 1 << 21, 2048)):
+        assert run(requests, tokens, heads) == _lib.ERR_BAD_SHAPE
+        assert cache.workspace_bytes(requests, tokens, heads, 1) == 0
+    rows = ctypes.byref(_lib.Rows(x.data_ptr(), 2, 256, 128))
+    assert lib.fp8_kv_append(cache._cache, _lib.MAX_REQUESTS + 1, 1, rows, rows, at, 1, at, at, None) == _lib.ERR_BAD_SHAPE
