@@ -260,6 +260,8 @@ class Fp8KVCache:
                 raise ValueError(f"out must have shape {tuple(q.shape)}, got {tuple(out.shape)}")
         if workspace is not None:
             _on_device(self.device, workspace=workspace)
+            if not workspace.is_contiguous():  # its bytes are counted from its elements
+                raise ValueError("workspace must be contiguous")
         if requests == 0 or tokens == 0:
             return out
         if table_pages == 0:  # no places at all: one page that is not named, so that rows of no request are left

@@ -11,7 +11,7 @@ import fp8_w8a8_quantized_token_amd as fp8
 from fp8_w8a8_quantized_token_amd import _lib
 from oracle import e4m3
 from tests._helpers import bf16_out_to_f64, require_gpu
-from tests.test_gpu_kv_cache import attend, make, reference
+from tests.test_gpu_kv_cache import attend, make, on_gpu, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,15 @@ def test_calls_beyond_the_limits_are_refused():
         assert cache.workspace_bytes(requests, tokens, heads, 1) == 0
     rows = ctypes.byref(_lib.Rows(x.data_ptr(), 2, 256, 128))
     assert lib.fp8_kv_append(cache._cache, _lib.MAX_REQUESTS + 1, 1, rows, rows, at, 1, at, at, None) == _lib.ERR_BAD_SHAPE
+
+
+def test_a_workspace_is_dense():
+    """Strided or broadcast elements are not as many bytes in a row."""
+    dev = require_gpu()
+    c = make([1], [4000], 2, 2, 128, 64, seed=44)
+    cache, *batch = on_gpu(c, dev)
+    need = cache.workspace_bytes(1, 1, 2, batch[0].shape[1])
+    assert need > 0
+    for ws in (torch.empty(1, dtype=torch.uint8, device=dev).expand(need), torch.empty(2 * need, dtype=torch.uint8, device=dev)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            cache.attend(c["q"].to(dev), *batch, workspace=ws)
