@@ -195,3 +195,18 @@ def test_a_workspace_is_dense():
     for ws in (torch.empty(1, dtype=torch.uint8, device=dev).expand(need), torch.empty(2 * need, dtype=torch.uint8, device=dev)[::2]):
         with pytest.raises(ValueError, match="contiguous"):
             cache.attend(c["q"].to(dev), *batch, workspace=ws)
+
+
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("counts", [[1], [1, 1, 1], [20, 1, 33], [300, 1, 1, 7], [1, 1, 900, 1]])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_table_much_wider_than_the_lengths(dim, counts, page):
+    """As a captured step holds it, and prompts beside single tokens: parts with nothing in them."""
+    dev = require_gpu()
+    c = make(counts, [n + 90 + 200 * i for i, n in enumerate(counts)], 4, 2, dim, page, seed=43)
+    wide = np.full((len(counts), 700), -1, np.int32)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = wide
+    # some rows have a token of 0.95 of the weight: the whole term, 2^-7 of the weight
+    for causal in (False, True):
+        assert_weighted(attend(c, dev, causal), *reference(c, causal))
