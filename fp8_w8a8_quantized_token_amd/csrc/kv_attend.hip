@@ -96,7 +96,7 @@ __device__ __forceinline__ v8bf widen(int w0, int w1) {
 // additions and the widening 20. Where a wavefront's softmax runs beside such products all the time
 // (kv_attend_teams) the additions are quicker (32760 x 32760, 16 heads of 128: 7.33 ms against 7.47;
 // 1560 x 32760: 438 us against 453), elsewhere the dot products (6 ragged causal requests, 32 heads
-// of 64: 123 us against 132). Sums of the unrounded p' would take 7.08 ms and 423 us.
+// of 64: 122 us against 131). Sums of the unrounded p' would take 7.08 ms and 423 us.
 template <int N, bool DOTS, class Scores>
 __device__ __forceinline__ float powers(const Scores& s, float c, float add, v8bf (&p)[N / 8]) {
   float sum[2] = {0.0f, 0.0f};
@@ -390,9 +390,9 @@ __device__ __forceinline__ void place(const AttendArgs& a, int& slot, int& kv, i
 // 2, 4 or 8 of these take turns with the slots of some heads and parts, so that each gets long and
 // short ones; who begins changes from one head and part to the next, so that all get nearly as many. (In
 // runs of neighbouring slots instead: 2 causal requests, 16380 and 8000 rows, 4 heads of 64 on 2 480
-// us against 300; 8 of up to 2000 on 6000, 20 heads of 128 on 5 441 against 394.) An XCD's unused
+// us against 300; 8 of up to 2000 on 6000, 20 heads of 128 on 5 466 against 401.) An XCD's unused
 // workgroups are its last: dealt out between the others they leave some of its CUs two (12 heads of
-// 128, 7800 rows on 7800: 514 us against 352).
+// 128, 7800 rows on 7800, 362 us: 1.46 times that).
 struct Deal {
   int slots, turns, each;  // log2 of the XCDs that take turns; heads and parts of each such set
 
@@ -575,8 +575,8 @@ __device__ __forceinline__ void tile_softmax(const AttendArgs& a, const Feed<DIM
 // cores would wait for them: 6 ragged causal requests of 32 heads 143 against 168 us. The
 // softmax in halves of 32 tokens, the output product of one under the exponentials of the
 // other: 149 against 146.5; four workgroups to a CU in 128 registers, with spills: 169.)
-// Bound by the vector instructions: of those 6 requests' 120 us they take 60% of all cycles,
-// products 32%, and 14% of the CUs' time passes before the first and after the last workgroups.
+// Bound by the vector instructions: of those 6 requests' 122 us they take 57% of all cycles,
+// products 31%, and 14% of the CUs' time passes before the first and after the last workgroups.
 template <int DIM, bool SMALL>
 __global__ __launch_bounds__(4 * DIM, 3) void kv_attend_tiles(AttendArgs a) {
   typedef Feed<DIM, SMALL> F;
@@ -652,9 +652,10 @@ __device__ __forceinline__ void phase_barrier() {
 // multiply(t + 1), by both teams, and written over three and four tiles later: each time after
 // the barrier that follows its last reader.
 //
-// Bound by power: at 32760 x 32760 and 16 heads an interval takes 1580 cycles, 1024 of them
-// products, and the clock, 2.4 GHz where it may, settles at 1.85 to 1.9 (1210 to 1240 TFLOP/s;
-// when an interval took 1930 cycles it stood at 2.04, and the whole was 3% slower).
+// Bound by power: at 32760 x 32760 and 16 heads a CU takes 1760 cycles for each of 8192 intervals, the
+// ends of its workgroups among them, 1024 of them products, and the clock, 2.4 GHz where it may,
+// settles at 1.93 (1180 to 1210 TFLOP/s; cycles that are saved come back in part only, since the
+// clock falls: 5% fewer are 3.4% of the time).
 template <int DIM, bool SMALL>
 __global__ __launch_bounds__(4 * DIM, 2) void kv_attend_teams(AttendArgs a) {
   typedef Feed<DIM, SMALL> F;
@@ -690,7 +691,7 @@ __global__ __launch_bounds__(4 * DIM, 2) void kv_attend_teams(AttendArgs a) {
       constexpr int kFrom = decltype(first)::value ? kOutProducts : 0;
       uint8_t* k_to = k_tile[k_slot == 0 ? 2 : k_slot - 1];
       uint8_t* v_to = v_tile[(t + 2) & 3];
-      // before the other team's vector work wherever both could issue (7.56 -> 7.30 ms)
+      // before the other team's vector work wherever both could issue (7.76 -> 7.40 ms)
       __builtin_amdgcn_s_setprio(1);
       s[0] = v16f{};
       s[1] = v16f{};
@@ -1011,9 +1012,12 @@ AttendCut kv_attend_cut(const KvCache& c, int64_t requests, int64_t tokens, int6
   const int64_t tiles = (table_pages * c.page_tokens + kTile - 1) / kTile;
   AttendCut x;
   // Up to 64 rows a request, some workgroups of 16 rows that each read its tokens are quicker than
-  // one that shares them through LDS with most of its 128 or 256 rows empty (16 heads of 128: 32
-  // rows of 32 requests on up to 4096 tokens 101 us against 184, 40 of 16 80 against 106, 60 of 16
-  // 104 against 100; of one request on 32760 tokens 24 rows 34 against 67, 64 55 against 70).
+  // one that shares them through LDS with most of its 128 or 256 rows empty (16 heads of 128 on up to
+  // 4096 tokens: up to 32 rows of 32 requests 100 us against 179, 40 of 16 67 against 102, 60 of 16 78
+  // against 106; of one request on 32760 tokens 24 rows 34 against 64, 64 55 against 68). The rule goes
+  // by rows alone: it gives grids that do not fill the CUs to the larger tiles although the smaller
+  // ones would be quicker there too (256 rows on 4096 27 us against 36; 1024 on 1024, 8 heads, 16
+  // against 32).
   const bool few = tokens * group <= 64 * requests;
   x.rows = few ? 16 : kThreadRows(4 * c.head_dim);
   x.shift = __builtin_ctz(x.rows);
@@ -1039,8 +1043,8 @@ AttendCut kv_attend_cut(const KvCache& c, int64_t requests, int64_t tokens, int6
   // In tiles' time. Heads of 128: rounds of one workgroup to a CU, each its share of the tiles
   // and what it starts and ends with (about 6 tiles). Heads of 64: three to a CU, which
   // together get through 1.4 times what one does. And the join: 2 tiles and the parts' way out
-  // and back. (1560 rows on 32760 tokens, 16 heads of 128: 1 part 697 us, 2 426, 4 441, 8 480; 256
-  // rows on 4096: 93, 60, 42 and 37.7; 2000 rows on 2000 tokens, 16 heads of 64: 1 part 37 us, 2 48.)
+  // and back. (1560 rows on 32760 tokens, 16 heads of 128: 1 part 740 us, 2 437, 4 450, 8 490; 256
+  // rows on 4096: 99, 62, 42 and 35.5; 2000 rows on 2000 tokens, 16 heads of 64: 1 part 36 us, 2 47.)
   const int at_once = (c.head_dim == 64 ? 3 : 1) * cus;
   auto rounds = [&](int64_t units, int p) {
     const double one = (double)tiles / p + 6, wgs = (double)units * p, all = std::ceil(wgs / at_once) * one;
@@ -1048,7 +1052,7 @@ AttendCut kv_attend_cut(const KvCache& c, int64_t requests, int64_t tokens, int6
   };
   // Where the last round of whole workgroups would be far from full (one request, whose tiles
   // take alike), its rows are a second launch in parts (4680 rows on 4680 tokens, 16 heads of 128,
-  // 304 workgroups: 247 -> 191 us; 2048 causal rows on 30000, 32 heads on 8: 905 -> 821 us).
+  // 304 workgroups: 252 -> 194 us).
   const int64_t full = requests == 1 ? busy / at_once * at_once / c.heads : 0;
   double best = 0;
   x.parts = 1;
