@@ -57,7 +57,7 @@ struct AttendArgs {
   const int32_t* table;
   const int32_t* lengths;
   uint16_t* out;    // [rows, heads, dim]
-  float* part_out;  // [parts, part_rows * heads, dim + 2]: a part's O / l, then m and l, where parts > 1
+  float* part_out;  // [parts, part_rows * heads, dim + 2]: a part's O, then m and l, where parts > 1
   int table_pages, heads, group, shift, causal, parts, slots;
   int skip;       // slots before this launch's first, served by another launch (of one request only)
   int part_rows;  // rows of part_out: the tensor's, or with skipped slots those that may be left of the request's
@@ -342,9 +342,8 @@ __device__ __forceinline__ bool find_span(const AttendArgs& a, int slot, int lan
 template <int DIM>
 __device__ __forceinline__ void store_rows(const AttendArgs& a, const Rows<DIM>& r, int64_t row_head, int part_row0,
                                            int part, int half) {
-  const float l = r.l;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   if (a.parts == 1) {
+    const float inv = r.l > 0.0f ? 1.0f / r.l : 0.0f;
     uint16_t* out = a.out + row_head * DIM + 16 * half;
 #pragma unroll
     for (int b = 0; b < DIM / 32; ++b)
@@ -365,11 +364,11 @@ __device__ __forceinline__ void store_rows(const AttendArgs& a, const Rows<DIM>&
 #pragma unroll
     for (int h = 0; h < 4; ++h)
       reinterpret_cast<float4*>(out + 32 * b + 16 * half)[h] =
-          make_float4(r.o[b][4 * h] * inv, r.o[b][4 * h + 1] * inv, r.o[b][4 * h + 2] * inv, r.o[b][4 * h + 3] * inv);
+          make_float4(r.o[b][4 * h], r.o[b][4 * h + 1], r.o[b][4 * h + 2], r.o[b][4 * h + 3]);
   if (half == 0) {
     float* ml = a.part_out + a.parts * all * DIM + (part * all + row_head) * 2;
     ml[0] = r.m;
-    ml[1] = l;
+    ml[1] = r.l;
   }
 }
 
@@ -897,7 +896,8 @@ __global__ __launch_bounds__(64 * NW, 3) void kv_attend_few(AttendArgs a) {
     wt[x] = __builtin_amdgcn_exp2f(join_m[x][lane] - top);
     sum += wt[x] * join_l[x][lane];
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  // a part leaves O as it is
+  const float inv = a.parts > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
   constexpr int kShare = DIM / 4 / NW;  // columns of a lane's DIM / 4
   const int64_t row_head = (int64_t)(w.row0 + token) * a.heads + head;
   const int column = (DIM / 4) * group + kShare * wave;
@@ -928,7 +928,8 @@ __global__ __launch_bounds__(64 * NW, 3) void kv_attend_few(AttendArgs a) {
   }
 }
 
-// The parts of each row and head joined: out = sum_i w_i O_i / sum_i w_i, w_i = l_i 2^(m_i - max m).
+// The parts of each row and head joined: out = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m).
+// (Of O_i / l_i and weights l_i 2^(m_i - max m) those under V scales of 2^100 would pass below fp32.)
 // One wavefront per row and head, lane i holding the weight of part i (at most kMaxParts). Rows
 // of no request, or of a skipped slot (the last tiles of the only request), were not written by
 // any part and are left alone. Eight parts are on their way at a time: bound by the parts' way
@@ -959,7 +960,7 @@ __global__ __launch_bounds__(256) void kv_attend_join(AttendArgs a, int row_shif
   float m = ml.x, sum = 0.0f;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  const float wt = ml.y * __builtin_amdgcn_exp2f(ml.x - m);
+  const float wt = __builtin_amdgcn_exp2f(ml.x - m), wl = wt * ml.y;
   const Cols* po = reinterpret_cast<const Cols*>(a.part_out + i * DIM) + lane;
   Cols o = {};
   for (int p0 = 0; p0 < a.parts; p0 += 8) {  // weights past the last part are zero
@@ -969,7 +970,7 @@ __global__ __launch_bounds__(256) void kv_attend_join(AttendArgs a, int row_shif
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float w = read_lane(wt, p0 + j);
-      sum += w;
+      sum += read_lane(wl, p0 + j);
       o += w * y[j];
     }
   }

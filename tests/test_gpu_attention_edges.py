@@ -23,12 +23,12 @@ def code_of(x):
     return int(e4m3.encode(np.array([x], np.float32))[0])
 
 
-def assert_weighted(got, ref, weight):
+def assert_weighted(got, ref, weight, slack=0.0, lost=0.0):
     """One rounding of each weight, shared by the sum that divides them, moves an output by up to
     2^-8 sum_j p_j |v_j - out| <= 2^-7 weight, its own rounding by 2^-8 of it; exponents of up to
-    2^7 in fp32 are off by less than 2^-15."""
+    2^7 in fp32 are off by less than 2^-15. `slack`: what the scores are off by besides."""
     err = np.abs(bf16_out_to_f64(got) - ref)
-    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -15) * weight
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -15 + slack) * weight + lost
     assert np.all(err <= bound), float(np.nanmax(err / (bound + 1e-300)))
 
 
@@ -210,3 +210,42 @@ def test_a_table_much_wider_than_the_lengths(dim, counts, page):
     # some rows have a token of 0.95 of the weight: the whole term, 2^-7 of the weight
     for causal in (False, True):
         assert_weighted(attend(c, dev, causal), *reference(c, causal))
+
+
+@pytest.mark.parametrize("page", [32, 64, 128])
+@pytest.mark.parametrize("count,dim", FORMS + [(20, 128), (500, 128)])
+@pytest.mark.parametrize("faint,size", [(-45, 110), (-35, 119), (-60, 60), (-60, -60), (-60, 0)])
+def test_faint_tokens_where_strong_ones_hold_zero(faint, size, count, dim, page):
+    """A column that the strongest token leaves at zero is made of tokens far below it, on places far away."""
+    dev = require_gpu()
+    c = make([count], [5000], 2, 1, dim, page, seed=45)
+    c["q"].zero_()
+    c["q"][..., 0] = 1.0
+    c["k"][:], c["v"][:], c["ks"][:], c["vs"][:] = 0, 0, 1.0, 2.0 ** size
+    for place, score, column in ((100, 100, 0), (2000, 100 + faint, 1), (4000, 100 + faint, 2)):
+        p = c["table"][0, place // page]
+        c["ks"][p] = score
+        c["k"][p, :, place % page, 0] = code_of(1.0)
+        c["v"][p, :, column, place % page] = code_of(1.0)
+    scale = float(np.float32(np.log(2.0)))  # a score of 1 is a power of two
+    got, (ref, weight) = attend(c, dev, scale=scale), reference(c, False, scale)
+    assert_weighted(got, ref, weight)
+    assert np.count_nonzero(bf16_out_to_f64(got)) == np.count_nonzero(ref) == 3 * 2 * count
+
+
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("count,dim", FORMS + [(20, 128), (500, 128)])
+@pytest.mark.parametrize("seed", range(6))
+def test_value_scales_anywhere_within_2_to_the_100(seed, count, dim, page):
+    """Random scales and scores of all sizes. What stands 2^-70 below a row's largest column may be lost to fp32."""
+    dev = require_gpu()
+    rng = np.random.default_rng(46 + seed)
+    c = make([count, 1], [1300, 900], 4, 2, dim, page, seed=47 + seed)
+    least = [-100, -60, -30, -5, 10, 19][seed]
+    c["vs"] = (2.0 ** rng.uniform(least, least + 100, c["vs"].shape)).astype(np.float32)
+    c["q"] *= 2.0 ** (seed - 1)
+    s = float(c["q"].double().abs().sum(-1).max()) * float(np.nanmax(c["ks"])) * 448 * dim ** -0.5
+    for causal in (False, True):
+        ref, weight = reference(c, causal)
+        # scores of this size in fp32: 2^-16 of their terms' sum, as in the tests of large scores
+        assert_weighted(attend(c, dev, causal), ref, weight, 2.0 ** -16 * s, 2.0 ** -70 * weight.max(-1, keepdims=True))
