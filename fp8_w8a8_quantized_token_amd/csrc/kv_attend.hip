@@ -119,6 +119,10 @@ __device__ __forceinline__ float powers(const Scores& s, float c, float add, v8b
   return sum[0] + sum[1];
 }
 
+// 2^x for x <= 0 in two equal factors: a product with both keeps what the power alone, zero below
+// 2^-126, would lose (a denominator may stand far above or below 1, see softmax_step).
+__device__ __forceinline__ float root_power(float x) { return __builtin_amdgcn_exp2f(0.5f * x); }
+
 // Only the first `live` of a lane's N tokens count.
 template <int N, class Scores>
 __device__ __forceinline__ void mask(const Scores& s, int live) {
@@ -129,7 +133,8 @@ __device__ __forceinline__ void mask(const Scores& s, int live) {
 // A tile's scores of N tokens per lane -> p', with m and l of the lane's row brought up to date
 // and O through `rescale`. s(e): the e-th score; c: score units of the tokens' page; lv, rv:
 // log2 and inverse of its V scale; `over`: the largest over the lanes that share a row; `first`:
-// no tile came before, so that the bound is sure to move.
+// no tile came before, so that the bound is sure to move. `rescale` multiplies O by the square of its
+// argument.
 template <int N, bool DOTS, class Scores, class Over, class Rescale>
 __device__ __forceinline__ void softmax_step(bool first, const Scores& s, float c, float lv, float rv, v8bf (&p)[N / 8],
                                              float& m, float& l, const Over& over, const Rescale& rescale) {
@@ -140,9 +145,9 @@ __device__ __forceinline__ void softmax_step(bool first, const Scores& s, float 
 #pragma unroll
     for (int e = 1; e < N; ++e) mx = fmaxf(mx, s(e));
     const float up = fmaxf(m, over(__builtin_fmaf(mx, c, fmaxf(lv, kLeastLog))));
-    const float fix = __builtin_amdgcn_exp2f(m - up);
+    const float fix = root_power(m - up);
     m = up;
-    l *= fix;
+    l = l * fix * fix;
     rescale(fix);
     sum = powers<N, DOTS>(s, c, lv - m, p);
   }
@@ -190,7 +195,7 @@ struct Rows {
 #pragma unroll
                                for (int b = 0; b < kOut; ++b)
 #pragma unroll
-                                 for (int e = 0; e < 16; ++e) o[b][e] *= fix;
+                                 for (int e = 0; e < 16; ++e) o[b][e] = o[b][e] * fix * fix;
                              });
   }
 };
@@ -859,7 +864,7 @@ __global__ __launch_bounds__(64 * NW, 3) void kv_attend_few(AttendArgs a) {
     };
     auto rescale = [&](float fix) {
 #pragma unroll
-      for (int b = 0; b < kOut; ++b) o[b] *= fix;
+      for (int b = 0; b < kOut; ++b) o[b] = o[b] * fix * fix;
     };
     if (some) {
       mask<16>(Tiles16{s}, id < 0 ? 0 : limit - at);
@@ -893,8 +898,8 @@ __global__ __launch_bounds__(64 * NW, 3) void kv_attend_few(AttendArgs a) {
   for (int x = 0; x < NW; ++x) top = fmaxf(top, join_m[x][lane]);
 #pragma unroll
   for (int x = 0; x < NW; ++x) {
-    wt[x] = __builtin_amdgcn_exp2f(join_m[x][lane] - top);
-    sum += wt[x] * join_l[x][lane];
+    wt[x] = root_power(join_m[x][lane] - top);
+    sum += wt[x] * join_l[x][lane] * wt[x];
   }
   // a part leaves O as it is
   const float inv = a.parts > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -906,7 +911,7 @@ __global__ __launch_bounds__(64 * NW, 3) void kv_attend_few(AttendArgs a) {
   for (int e = 0; e < kShare; ++e) {
     float z = 0.0f;
 #pragma unroll
-    for (int x = 0; x < NW; ++x) z += wt[x] * join_o[x][lane][kShare * wave + e];
+    for (int x = 0; x < NW; ++x) z += wt[x] * join_o[x][lane][kShare * wave + e] * wt[x];
     y[e] = z * inv;
   }
   if (a.parts == 1) {
@@ -960,7 +965,7 @@ __global__ __launch_bounds__(256) void kv_attend_join(AttendArgs a, int row_shif
   float m = ml.x, sum = 0.0f;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  const float wt = __builtin_amdgcn_exp2f(ml.x - m), wl = wt * ml.y;
+  const float wt = root_power(ml.x - m), wl = wt * ml.y * wt;
   const Cols* po = reinterpret_cast<const Cols*>(a.part_out + i * DIM) + lane;
   Cols o = {};
   for (int p0 = 0; p0 < a.parts; p0 += 8) {  // weights past the last part are zero
@@ -971,7 +976,7 @@ __global__ __launch_bounds__(256) void kv_attend_join(AttendArgs a, int row_shif
     for (int j = 0; j < 8; ++j) {
       const float w = read_lane(wt, p0 + j);
       sum += read_lane(wl, p0 + j);
-      o += w * y[j];
+      o += w * y[j] * w;
     }
   }
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;

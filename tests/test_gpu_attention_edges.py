@@ -249,3 +249,26 @@ def test_value_scales_anywhere_within_2_to_the_100(seed, count, dim, page):
         ref, weight = reference(c, causal)
         # scores of this size in fp32: 2^-16 of their terms' sum, as in the tests of large scores
         assert_weighted(attend(c, dev, causal), ref, weight, 2.0 ** -16 * s, 2.0 ** -70 * weight.max(-1, keepdims=True))
+
+
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("count,dim", FORMS + [(20, 128), (500, 128)])
+@pytest.mark.parametrize("first", [512, 64])
+def test_weights_below_a_bound_that_jumps(first, count, dim, page):
+    """Tokens of tiny values whose weight, 2^3 of that of the tokens of large values behind them, is all in the
+    denominator: the bound of the row rises by 2^127 in between."""
+    dev = require_gpu()
+    c = make([count], [1300], 2, 1, dim, page, seed=48)
+    c["q"].zero_()
+    c["q"][..., 0] = 1.0
+    c["k"][:] = 0
+    for j, p in enumerate(c["table"][0, :-(-1300 // page)]):
+        if j * page < first:  # sets the bound of the row to 0
+            c["vs"][p], c["ks"][p] = 2.0 ** -60, 60
+            c["k"][p, :, :, 0] = code_of(1.0)
+        else:
+            late = j * page >= 1024
+            c["vs"][p], c["ks"][p] = 2.0 ** (40 if late else -60), 87 if late else 90
+            c["k"][p, :, 7, 0] = code_of(1.0)
+    scale = float(np.float32(np.log(2.0)))
+    assert_weighted(attend(c, dev, scale=scale), *reference(c, False, scale))
