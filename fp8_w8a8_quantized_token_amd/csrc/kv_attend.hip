@@ -658,7 +658,7 @@ __device__ __forceinline__ void phase_barrier() {
 //
 // Bound by power: at 32760 x 32760 and 16 heads a CU takes 1760 cycles for each of 8192 intervals, the
 // ends of its workgroups among them, 1024 of them products, and the clock, 2.4 GHz where it may,
-// settles at 1.93 (1180 to 1210 TFLOP/s; cycles that are saved come back in part only, since the
+// settles at 1.9 (1165 to 1210 TFLOP/s; cycles that are saved come back in part only, since the
 // clock falls: 5% fewer are 3.4% of the time).
 template <int DIM, bool SMALL>
 __global__ __launch_bounds__(4 * DIM, 2) void kv_attend_teams(AttendArgs a) {
