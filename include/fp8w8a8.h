@@ -581,7 +581,8 @@ int fp8_kv_append(const fp8_kv_cache* cache, int64_t requests, int64_t tokens, c
  * stands in slots that a row does not see, NaN codes and the scales of pages it sees nothing
  * of included, has no effect on it. Queries and what a row sees must be finite (a NaN among it
  * may reach the output or not), the scales of both above 0, and the V scales of one request
- * between 2^-100 and 2^119 and within 2^100 of each other.
+ * between 2^-100 and 2^119 and within 2^100 of each other. What adds less than 2^-70 of a row's
+ * largest column to another may be lost to the range of fp32.
  *
  *   q          fp8_rows, heads a multiple of the cache's. A launch holds fewer than 2^23
  *              workgroups: tokens * heads / 16 + requests * cache heads up to 2^22 always fits,
